@@ -984,7 +984,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // same TMEM lane, so a warp adds them by itself: warps of chain 0 take the first half of
                 // the columns, those of chain 1 the second; repeats go through shared memory, each warp
                 // keeping kOwn of its columns and giving the rest to the warps that keep those.
+                // A chain without a tile in the next unit gets to its write of `stats` there without
+                // waiting for the other chain's warps, which may have to read this unit's sums still.
+                // Repeats meet again further down; without them the warps arrive once more behind
+                // their reads, and wait for that arrival before they write the next unit's sums.
                 float2 *stats = reinterpret_cast<float2 *>(smem + L::kStats);
+                if (kSplit == 1 && joins > 0 && !(ok = warp_wait(bar(L::bJoin), (joins - 1) & 1, wc, 14))) break;
                 stats[x * 128 + ln] = make_float2(base, l);
                 if (!(ok = sync())) break;
                 float top = -INFINITY, all = 0.f, f[2];
@@ -1004,6 +1009,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const float2 v = stats[y * 128 + ln];
                     f[y] = v.y > 0.f ? ex2_approx(v.x - top) : 0.f;
+                }
+                if constexpr (kSplit == 1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(L::bJoin));
+                    ++joins;
                 }
                 const bool two = n > 1;  // chain 1 has a tile
                 ok = warp_wait(bar(L::bOFull + 0), uo0 & 1, wc, 12) &&
