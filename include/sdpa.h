@@ -437,6 +437,9 @@ size_t sdpa_tree_fwd_workspace_size(int num_seqs, int max_seqlen_q,
  *   included; what some row sees must be finite.  Rows of o and lse behind
  *   cu[num_seqs] are left as they were.
  *   max_seqlen_q, max_seqlen_kv : upper bounds of n and of kv_lens.
+ *   P enters the second product rounded to dtype (2^-8 of itself for bf16; for
+ *     fp16 2^-11, or 2^-32 of the row's largest P where that is more); its sum is
+ *     taken unrounded.  E4M3 caches: see below.
  *   descale_k, descale_v : fp32 scalars in device memory for an E4M3 cache,
  *     code * descale being the value; ignored otherwise (may be NULL).  Q and
  *     P are not rounded to 8 bits but split into 8-bit terms: Q is exact to

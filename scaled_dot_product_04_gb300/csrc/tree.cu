@@ -738,10 +738,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float descale_v = kFp8 ? *p.descale_v : 1.f;
         const int tok_l = row / p.group;           // the row's token in the chain's tile
         // P is exp2(x - base).  base follows the running maximum with a lag of
-        // up to kLag (log2), so O is seldom rescaled; an E4M3 cache's P is
-        // raised by 2^kRaise so that small weights keep their terms, up to
-        // 2^11.5, whose rest of at most 2^8 still is an E4M3 value
-        constexpr float kRaise = kFp8 ? 8.f : 0.f, kLag = kFp8 ? 3.5f : 8.f;
+        // up to kLag (log2), so O is seldom rescaled.  P is raised by 2^kRaise
+        // so that small weights keep their bits: fp16 to at most 2^15, which
+        // leaves weights off by up to 2^-32 of the row's largest and not
+        // 2^-25 (30,000 keys of such a weight are a thousandth of O); an E4M3
+        // cache's terms up to 2^11.5, whose rest of at most 2^8 still is an
+        // E4M3 value; bf16 has fp32's exponents
+        constexpr float kRaise = kFp8 ? 8.f : kBf16 ? 0.f : 7.f, kLag = kFp8 ? 3.5f : 8.f;
         int it = 0, units = 0, cnt = 0, uo0 = 0, uo1 = 0, joins = 0;
         bool ok = true;
         __syncthreads();

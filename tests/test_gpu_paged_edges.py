@@ -1,9 +1,12 @@
 """Edges of the paged-cache operators on the GPU: orders between units, weights near the types' ends, sizes near
 32 bits.  Bounds and helpers are those of test_gpu_paged.
 """
+import math
+
 import pytest
 import torch
 
+import paged_refs
 import test_gpu_paged as base
 from test_gpu_paged import sdpa  # noqa: F401  (fixture)
 
@@ -28,3 +31,40 @@ def test_units_of_one_tile_behind_units_of_more(sdpa, fp8):  # noqa: F811
     for _ in range(60):
         x, y = base._call(sdpa, c)
         assert torch.equal(x, o) and torch.equal(y, lse)
+
+
+# ------------------------------------------------------------------ weights near the types' ends
+@pytest.mark.parametrize("n", [1, 9, 20, 40], ids=["rows_32", "rows_64", "rows_256", "both"])
+def test_fp16_weights_far_below_a_sink_of_no_value(sdpa, n):  # noqa: F811
+    """The first keys' one takes nearly all the weight and its value is zero, so O comes from 30,000 keys whose
+    weights are near 2^-25 of the largest.  152 requests share the pages, so that a CTA sums a long run of keys under
+    the sink's maximum.  P is raised by 2^7 at least before it is rounded to fp16: half a step is 2^-11 of a weight,
+    and where P is below fp16's normal range 2^-25, which is 2^-32 of the row's largest weight (a weight never loses
+    more than itself).  So |dO| <= 2^-11 A + sum_j min(w_ij, 2^-32 max_j w_ij) |v_j|, beside the other terms."""
+    size, h, b = 30000, 4, 152
+    c = base._attend_case(7, [size], [n], h, 1, 128, 64, HF, tree=False)
+    scores = torch.tensor([23.0, 24.5, 25.2, 26.0], dtype=torch.float64) * math.log(2.0)
+    q = torch.zeros(n, h, 128, device="cuda")
+    q[:, :, 0] = scores.float().cuda()
+    c["q"], c["scale"] = q.to(HF), 1.0
+    c["kc"][..., 0] = 0.0
+    c["vc"] = c["vc"].abs() + 0.5
+    sink = c["table"][0][0], 5
+    c["kc"][sink[0], 0, sink[1], 0] = 1.0
+    c["vc"][sink[0], 0, sink[1]] = 0.0
+    k = paged_refs.keys_of(c["kc"].cpu(), c["table"][0], size)[0]
+    v = paged_refs.keys_of(c["vc"].cpu(), c["table"][0], size)[0]
+    s = torch.einsum("nhd,jd->nhj", c["q"].cpu().double(), k)
+    s = s.masked_fill(torch.arange(size)[None, None] > (size - n + torch.arange(n))[:, None, None], -math.inf)
+    w = torch.softmax(s, -1)
+    ref = w @ v
+    least = torch.minimum(w, w.amax(-1, keepdim=True) * 2.0 ** -32) @ v
+    big = s.amax().item()
+    bound = (2.0 ** -11 + 2 * (big + 16) * 2.0 ** -21) * ref + least + 2.0 ** -11 * ref + 2.0 ** -25
+    c["q"], c["table"], c["lens"], c["cu"] = c["q"].repeat(b, 1, 1), c["table"] * b, [size] * b, [n * i for i in range(b + 1)]
+    o, lse = base._call(sdpa, c)
+    sdpa.sdpa_check_device_error()
+    off = ((o.cpu().double().view(b, n, h, 128) - ref).abs() / bound).max().item()
+    assert off <= 1.0, f"O is {off:.2f} times its bound off"
+    off = (lse.cpu().double().view(b, n, h) - torch.logsumexp(s, -1)).abs().max().item()
+    assert off <= (2 * big + 16) * 2.0 ** -21
