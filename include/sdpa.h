@@ -436,7 +436,9 @@ size_t sdpa_tree_fwd_workspace_size(int num_seqs, int max_seqlen_q,
  *   and new tokens that no row of their request sees, may hold anything, NaN
  *   included; what some row sees must be finite.  Rows of o and lse behind
  *   cu[num_seqs] are left as they were.
- *   max_seqlen_q, max_seqlen_kv : upper bounds of n and of kv_lens.
+ *   max_seqlen_q, max_seqlen_kv : upper bounds of n and of kv_lens.  A table
+ *     holds fewer than 2^31 - 128 keys a request, and a launch is refused whose
+ *     key tiles of 128, by these bounds and over all row tiles, come near 2^30.
  *   P enters the second product rounded to dtype (2^-8 of itself for bf16; for
  *     fp16 2^-11, or 2^-32 of the row's largest P where that is more); its sum is
  *     taken unrounded.  E4M3 caches: see below.

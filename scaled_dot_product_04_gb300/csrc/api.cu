@@ -1210,8 +1210,9 @@ int sdpa_tree_fwd(const void *q, const void *k_cache, const void *v_cache, void 
     if ((st = check_stride(q_stride, h, d, "q_stride"))) return st;
     if (total_q == 0 || h == 0) return ok();
     if (num_pages == 0) return fail(SDPA_ERR_INVALID_ARG, "num_pages is 0");
+    // the end of a table's last key tile is a 31-bit number too
     if ((int64_t)num_seqs * max_blocks > INT32_MAX || (int64_t)total_q * h > INT32_MAX ||
-        (int64_t)max_blocks * page_size > INT32_MAX ||
+        (int64_t)max_blocks * page_size > INT32_MAX - kTileN ||
         tree_places(max_seqlen_q, total_q, num_seqs, h_kv, h / h_kv, max_seqlen_kv) > INT32_MAX)
         return fail(SDPA_ERR_INVALID_ARG, "problem too large for one launch");
     const size_t cb = cache_bytes(num_pages, h_kv, page_size, d, cache_dtype);

@@ -1281,8 +1281,9 @@ static int64_t tree_units(int max_q, int total_q, int num_seqs, int h_kv, int gr
     const int tokens = (rows == 256 ? 2 : 1) * ((rows == 256 ? 128 : rows) / group);
     return ((int64_t)total_q / tokens + num_seqs) * h_kv;
 }
+static int64_t tree_tiles(int max_kv) { return ((int64_t)max_kv + kTileN - 1) / kTileN + 1; }  // of a unit
 int64_t tree_places(int max_q, int total_q, int num_seqs, int h_kv, int group, int max_kv) {
-    const int64_t units = tree_units(max_q, total_q, num_seqs, h_kv, group), tiles = (max_kv + kTileN - 1) / kTileN + 1;
+    const int64_t units = tree_units(max_q, total_q, num_seqs, h_kv, group), tiles = tree_tiles(max_kv);
     return units > INT32_MAX ? units : units * (2 * tiles + 8);
 }
 
@@ -1296,7 +1297,7 @@ cudaError_t launch_tree_fwd(const CUtensorMap &tq, const CUtensorMap &tk, const 
                             int cache_dtype, int sm_count, cudaStream_t stream, const KernelTimer &timer) {
     const int rows = tree_rows(max_q, p.group);
     // no more CTAs than key tiles there can be
-    const int64_t tiles = tree_units(max_q, p.total_q, p.num_seqs, p.h_kv, p.group) * ((p.max_kv + kTileN - 1) / kTileN + 1);
+    const int64_t tiles = tree_units(max_q, p.total_q, p.num_seqs, p.h_kv, p.group) * tree_tiles(p.max_kv);
     const int grid = (int)(tiles < sm_count ? tiles : sm_count < kTreeMaxCtas ? sm_count : kTreeMaxCtas);
 #define SDPA_TREE_CASE(D_, EL_, FP8_)                                  \
     if (p.d == D_ && dtype == EL_ && (cache_dtype == kElE4m3) == FP8_) \

@@ -68,3 +68,16 @@ def test_fp16_weights_far_below_a_sink_of_no_value(sdpa, n):  # noqa: F811
     assert off <= 1.0, f"O is {off:.2f} times its bound off"
     off = (lse.cpu().double().view(b, n, h) - torch.logsumexp(s, -1)).abs().max().item()
     assert off <= (2 * big + 16) * 2.0 ** -21
+
+
+# ------------------------------------------------------------------ sizes near 32 bits
+@pytest.mark.parametrize("bound", [2 ** 31 - 1, 2 ** 31 - 128, 2 ** 24])
+def test_a_generous_bound_of_the_lengths(sdpa, bound):  # noqa: F811
+    """max_seqlen_kv may be any upper bound."""
+    c = base._attend_case(8, [700, 33], [9, 3], 8, 2, 128, 16, BF)
+    o, lse = base._call(sdpa, c)
+    mask = paged_refs.words_of(c["rows"], c["words"]).cuda()
+    x, y = sdpa.attention_tree(c["q"], c["kc"], c["vc"], base._i32(c["table"]), base._i32(c["cu"]), base._i32(c["lens"]),
+                               9, bound, tree_mask=mask, scale=c["scale"])
+    sdpa.sdpa_check_device_error()
+    assert torch.equal(x, o) and torch.equal(y, lse)

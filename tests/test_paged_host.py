@@ -144,3 +144,19 @@ def test_python_refuses_what_pointers_cannot_say():
     with pytest.raises(sdpa.SdpaError) as e:
         sdpa.cache_append(k, k, cache.float(), cache.float(), slots)
     assert e.value.status == L.SDPA_ERR_UNSUPPORTED
+
+
+INT_MAX = 2 ** 31 - 1
+
+
+def test_tree_bounds_near_32_bits_are_counted_in_64(lib):
+    """max_seqlen_kv is any upper bound: the key tiles that it allows are counted without overflow, and a list of
+    them past 31 bits is refused; so is a table whose last tile would end past 31 bits."""
+    from scaled_dot_product_04_gb300 import _lib as L
+    for kw in [dict(b=100, total=100, mq=1, mkv=INT_MAX),
+               dict(b=100, total=100, mq=1, mkv=INT_MAX - 100),
+               dict(b=4000, total=4000, mq=1, mkv=INT_MAX - 126),
+               dict(b=1, mkv=100, blocks=(1 << 27) - 1, page=16),
+               dict(b=1, mkv=100, blocks=(1 << 24) - 1, page=128)]:
+        assert _tree(lib, **kw) == L.SDPA_ERR_INVALID_ARG, (kw, L.sdpa_last_error())
+        assert "too large for one launch" in L.sdpa_last_error(), (kw, L.sdpa_last_error())
