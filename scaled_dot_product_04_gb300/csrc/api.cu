@@ -1052,7 +1052,7 @@ int sdpa_cache_plan(const int32_t *ctx_lens, const int32_t *new_lens, const int3
         return fail(SDPA_ERR_INVALID_ARG, "negative size (num_seqs=%d max_blocks=%d max_new=%d mask_words=%d)",
                     num_seqs, max_blocks, max_new, mask_words);
     if (num_pages == 0) return fail(SDPA_ERR_INVALID_ARG, "num_pages is 0");
-    if (max_new > (1 << 30) || (int64_t)num_seqs * max_blocks > INT32_MAX || (int64_t)max_blocks * page_size > INT32_MAX)
+    if (max_new > (1 << 30) || num_seqs > (1 << 30) || (int64_t)num_seqs * max_blocks > INT32_MAX || (int64_t)max_blocks * page_size > INT32_MAX)
         return fail(SDPA_ERR_INVALID_ARG, "problem too large for one launch");
     if (tree_mask && (!parents || mask_words == 0))
         return fail(SDPA_ERR_INVALID_ARG, "tree_mask needs parents and mask_words > 0");

@@ -160,3 +160,11 @@ def test_tree_bounds_near_32_bits_are_counted_in_64(lib):
                dict(b=1, mkv=100, blocks=(1 << 24) - 1, page=128)]:
         assert _tree(lib, **kw) == L.SDPA_ERR_INVALID_ARG, (kw, L.sdpa_last_error())
         assert "too large for one launch" in L.sdpa_last_error(), (kw, L.sdpa_last_error())
+
+
+def test_plan_refuses_more_requests_than_its_scan_counts(lib):
+    """With no table columns, the table's size alone does not bound the requests."""
+    from scaled_dot_product_04_gb300 import _lib as L
+    for b in ((1 << 30) + 1, INT_MAX):
+        assert _plan(lib, b=b, blocks=0) == L.SDPA_ERR_INVALID_ARG, L.sdpa_last_error()
+        assert "too large for one launch" in L.sdpa_last_error()
