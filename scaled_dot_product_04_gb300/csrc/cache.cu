@@ -26,7 +26,8 @@ SDPA_DEV void report_bad_data(uint32_t *err, uint32_t tag, uint32_t site) {
 // prompts of 520,000 tokens in all 7.1 us, launch and host included.
 constexpr int kPlanThreads = 256, kPlanTokens = 8;
 
-// Sum of non-negative counts that stays at `cap` once it gets there.
+// Sum of non-negative counts that stays at `cap` once it gets there (pages given back: at the
+// pages there are, whatever the requests claim to hold).
 SDPA_DEV int sat_add(int a, int b, int cap) { return a > cap - b ? cap : a + b; }
 
 struct Request {
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p, 
         const Request q = load_request(p, r);
         n = sat_add(n, q.n, p.max_new);
         w += q.want;
-        back += q.back;
+        back = sat_add(back, q.back, p.num_pages);
         over = sat_add(over, q.over, INT32_MAX);
     }
     // inclusive scans of n, w and back over the warp, then over the warps
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p, 
         if (lane >= off) {
             in = sat_add(in, a, p.max_new);
             iw += c;
-            ib += e;
+            ib = sat_add(ib, e, p.num_pages);
         }
         over = sat_add(over, f, INT32_MAX);
     }
@@ -129,11 +130,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p, 
     for (int i = 0; i < warp; ++i) {
         bn = sat_add(bn, s_warp[0][i], p.max_new);
         bw += s_warp[1][i];
-        bb += s_warp[2][i];
+        bb = sat_add(bb, s_warp[2][i], p.num_pages);
     }
     s_n[tid + 1] = sat_add(bn, in, p.max_new);
     s_w[tid + 1] = bw + iw;
-    s_b[tid + 1] = bb + ib;
+    s_b[tid + 1] = sat_add(bb, ib, p.num_pages);
     if (tid == 0) s_n[0] = s_w[0] = s_b[0] = 0;
     __syncthreads();
     const int total = s_n[kPlanThreads], wanted = s_w[kPlanThreads], returned = s_b[kPlanThreads];
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p, 
             const Request q = load_request(p, i);
             first_n = sat_add(first_n, q.n, p.max_new);
             first_w += q.want;
-            first_b += q.back;
+            first_b = sat_add(first_b, q.back, pages);
         }
         const Request q = load_request(p, r);
         const int granted = min(max(count - first_w, 0), q.want);
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p, 
         }
         for (int j = lane; j < q.want; j += 32)
             row[q.held + j] = j < granted ? p.free_ring[ring_at(first_w + j)] : -1;
-        // pages given back go behind the free entries that were there
+        // pages given back go behind the free entries that were there, as far as the ring has room
         for (int j = lane; j < q.back; j += 32)
             if (count + first_b + j < pages) p.free_ring[ring_at(count + first_b + j)] = row[j];
     }
@@ -215,8 +216,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p, 
                 page_row = r;
                 page = -1;
                 if (blk < q.held) page = p.table[(int64_t)r * p.max_blocks + blk];
-                else if (blk < p.max_blocks && first_w + blk - q.held < count)
-                    page = p.free_ring[ring_at(first_w + blk - q.held)];
+                else if (blk < p.max_blocks && first_w + (blk - q.held) < count)
+                    page = p.free_ring[ring_at(first_w + (blk - q.held))];
                 if (page >= pages) page = -1;
             }
             if (page >= 0) slot[e] = page * p.page_size + at - blk * p.page_size;

@@ -81,3 +81,19 @@ def test_a_generous_bound_of_the_lengths(sdpa, bound):  # noqa: F811
                                9, bound, tree_mask=mask, scale=c["scale"])
     sdpa.sdpa_check_device_error()
     assert torch.equal(x, o) and torch.equal(y, lse)
+
+
+def test_plan_takes_back_no_more_pages_than_there_are(sdpa):  # noqa: F811
+    """Requests that claim to hold 2^31 - 16 pages in all, sixteen times what exists: the returned pages that the
+    ring has room for are taken, in order, and the count of the rest does not wrap."""
+    b, blocks = 16, (1 << 27) - 1
+    pages = blocks
+    ring = torch.full((pages,), -3, dtype=torch.int32, device="cuda")
+    table = torch.zeros(b, blocks, dtype=torch.int32, device="cuda")
+    table[0, :5] = base._i32([7, 1, 4, 2, 9])
+    got = sdpa.cache_plan(base._i32([0] * b), base._i32([-1] * b), base._i32([blocks] * b), base._i32([3, pages - 5, 0]), ring, table, 16, 0)
+    torch.cuda.synchronize()
+    assert got.ring_state.tolist() == [3, pages, 0] and got.held.tolist() == [0] * b
+    assert ring[pages - 2:].tolist() == [7, 1] and ring[:3].tolist() == [4, 2, 9]
+    assert (ring[3:pages - 2] == -3).all().item()
+    assert table[0, :5].tolist() == [7, 1, 4, 2, 9] and not table[1:].any().item()
