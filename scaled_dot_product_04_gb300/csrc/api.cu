@@ -1146,8 +1146,9 @@ int sdpa_cache_accept(void *k_cache, void *v_cache, const int32_t *block_table,
     if (st) return st;
     if (num_seqs < 0 || max_blocks < 0 || max_path < 0)
         return fail(SDPA_ERR_INVALID_ARG, "negative size (num_seqs=%d max_blocks=%d max_path=%d)", num_seqs, max_blocks, max_path);
+    const int row_bytes = d * (cache_dtype == SDPA_FP8_E4M3 ? 1 : 2);
     if ((int64_t)num_seqs * max_blocks > INT32_MAX || (int64_t)num_seqs * max_path > INT32_MAX ||
-        (int64_t)max_blocks * page_size > INT32_MAX)
+        (int64_t)max_blocks * page_size > INT32_MAX || 2 * (int64_t)h_kv * (row_bytes / 16) > kAcceptMaxColumns)
         return fail(SDPA_ERR_INVALID_ARG, "problem too large for one launch");
     if (num_seqs == 0 || h_kv == 0) return ok();
     const size_t cb = cache_bytes(num_pages, h_kv, page_size, d, cache_dtype), per = (size_t)num_seqs * 4;
@@ -1171,7 +1172,7 @@ int sdpa_cache_accept(void *k_cache, void *v_cache, const int32_t *block_table,
     p.max_blocks = max_blocks;
     p.max_path = max_path;
     p.h_kv = h_kv;
-    p.row_bytes = d * (cache_dtype == SDPA_FP8_E4M3 ? 1 : 2);
+    p.row_bytes = row_bytes;
     p.num_pages = num_pages;
     p.page_size = page_size;
     return launch_status(launch_cache_accept(p, static_cast<cudaStream_t>(stream)), "sdpa_cache_accept");

@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
 // 1000 requests that keep up to 12 of 64 nodes, 8 heads, bf16: 8.2 us, 4.9 TB/s
 // (two rows ahead 9.6, eight 9.1, sixteen 12.1; 256 threads 8.5; one row after the
 // other with its own look-ups 18.5).
-constexpr int kAcceptThreads = 128, kAcceptAhead = 4;
+constexpr int kAcceptAhead = 4;
 
 __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptParams p) {
     __shared__ int64_t s_from[kAcceptThreads], s_to[kAcceptThreads];  // row numbers of head 0, from < 0: no move

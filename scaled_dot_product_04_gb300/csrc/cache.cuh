@@ -53,6 +53,8 @@ struct AcceptParams {
     uint32_t *err;
     int b, max_blocks, max_path, h_kv, row_bytes, num_pages, page_size;
 };
+constexpr int kAcceptThreads = 128;  // a 16-byte column each, of a row of the two caches
+constexpr int64_t kAcceptMaxColumns = 65535ll * kAcceptThreads;  // the CTAs of a grid's y
 cudaError_t launch_cache_accept(const AcceptParams &p, cudaStream_t stream);
 
 // Attention of new tokens over the cache (sdpa_tree_fwd).

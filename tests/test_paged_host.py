@@ -168,3 +168,12 @@ def test_plan_refuses_more_requests_than_its_scan_counts(lib):
     for b in ((1 << 30) + 1, INT_MAX):
         assert _plan(lib, b=b, blocks=0) == L.SDPA_ERR_INVALID_ARG, L.sdpa_last_error()
         assert "too large for one launch" in L.sdpa_last_error()
+
+
+def test_accept_refuses_rows_wider_than_a_grid(lib):
+    """A launch has 65,535 CTAs of 128 16-byte columns over the heads of both caches."""
+    from scaled_dot_product_04_gb300 import _lib as L
+    most = 65535 * 128 // (2 * 16)  # d = 128, 16 bits: 16 columns a row
+    for h in (most + 1, 1 << 27):
+        assert _accept(lib, h_kv=h, pages=0) == L.SDPA_ERR_INVALID_ARG, L.sdpa_last_error()
+        assert "too large for one launch" in L.sdpa_last_error()
