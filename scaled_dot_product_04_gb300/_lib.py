@@ -143,9 +143,9 @@ def calls():
         import importlib.util
         import torch  # noqa: F401  (the module links against it)
         lib = load()
-        path = _build.build_calls()
-        with _lock:
+        with _lock:  # another thread's first call waits here
             if _calls is None:
+                path = _build.build_calls()
                 spec = importlib.util.spec_from_file_location("_sdpa_calls", path)
                 module = importlib.util.module_from_spec(spec)
                 spec.loader.exec_module(module)

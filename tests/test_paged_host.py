@@ -177,3 +177,67 @@ def test_accept_refuses_rows_wider_than_a_grid(lib):
     for h in (most + 1, 1 << 27):
         assert _accept(lib, h_kv=h, pages=0) == L.SDPA_ERR_INVALID_ARG, L.sdpa_last_error()
         assert "too large for one launch" in L.sdpa_last_error()
+
+
+def test_first_use_from_two_threads_builds_once(monkeypatch):
+    """Two threads' first calls: one build at a time, one module."""
+    import threading
+    import time
+
+    from scaled_dot_product_04_gb300 import _lib as L
+    L.calls()
+    running, most, lock = [0], [0], threading.Lock()
+    path = L._build.build_calls()
+
+    def build_calls():
+        with lock:
+            running[0] += 1
+            most[0] = max(most[0], running[0])
+        time.sleep(0.2)
+        with lock:
+            running[0] -= 1
+        return path
+
+    monkeypatch.setattr(L, "_calls", None)
+    monkeypatch.setattr(L._build, "build_calls", build_calls)
+    got = []
+    threads = [threading.Thread(target=lambda: got.append(L.calls())) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert len(got) == 4 and all(m is got[0] for m in got) and most[0] == 1
+
+
+def test_compilers_of_two_threads_write_to_different_files(monkeypatch, tmp_path):
+    """Whoever builds at the same time as another installs a module that is whole."""
+    import threading
+
+    from scaled_dot_product_04_gb300 import build
+    calls = tmp_path / "_sdpa_calls.so"
+    monkeypatch.setattr(build, "CALLS", str(calls))
+    written, meet = [], threading.Barrier(2)
+
+    def run(cmd, **kw):
+        out = cmd[cmd.index("-o") + 1]
+        written.append(out)
+        with open(out, "w") as f:
+            f.write("whole")
+        meet.wait(30)
+        return type("Done", (), {"returncode": 0, "stdout": "", "stderr": ""})()
+
+    monkeypatch.setattr(build.subprocess, "run", run)
+    failed = []
+
+    def one():
+        try:
+            build.build_calls(force=True)
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=one) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not failed and len(set(written)) == 2 and calls.read_text() == "whole"
