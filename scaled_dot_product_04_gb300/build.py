@@ -48,13 +48,18 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
-def calls_up_to_date() -> bool:
+def _calls_stamp() -> str:
+    import sysconfig
     import torch
-    stamp = CALLS + ".torch"  # the module goes with the torch it was built against
+    return f"{torch.__version__} {sysconfig.get_config_var('SOABI')}"
+
+
+def calls_up_to_date() -> bool:
+    stamp = CALLS + ".torch"  # the module goes with the torch and the Python it was built against
     if not (os.path.exists(CALLS) and os.path.exists(stamp)):
         return False
     with open(stamp) as f:
-        if f.read() != torch.__version__:
+        if f.read() != _calls_stamp():
             return False
     t = os.path.getmtime(CALLS)
     return all(os.path.getmtime(p) <= t for p in (CALLS_SRC, os.path.join(ROOT, "include", "sdpa.h"), __file__))
@@ -81,7 +86,7 @@ def build_calls(force: bool = False) -> str:
         raise RuntimeError(f"compiling {CALLS_SRC} failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CALLS)
     with open(CALLS + ".torch", "w") as f:
-        f.write(torch.__version__)
+        f.write(_calls_stamp())
     return CALLS
 
 

@@ -241,3 +241,15 @@ def test_compilers_of_two_threads_write_to_different_files(monkeypatch, tmp_path
     for t in threads:
         t.join(60)
     assert not failed and len(set(written)) == 2 and calls.read_text() == "whole"
+
+
+def test_the_compiled_entry_goes_with_its_python(monkeypatch):
+    """A module built for another Python is not taken for an up-to-date one."""
+    import sysconfig
+
+    from scaled_dot_product_04_gb300 import build
+    build.build_calls()
+    assert build.calls_up_to_date()
+    real = sysconfig.get_config_var
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda name: "cpython-399-other" if name == "SOABI" else real(name))
+    assert not build.calls_up_to_date()
