@@ -1133,7 +1133,7 @@ int sdpa_cache_append(const void *k, const void *v, void *k_cache, void *v_cache
     p.d = d;
     p.num_pages = num_pages;
     p.page_size = page_size;
-    return launch_status(launch_cache_append(p, dtype, cache_dtype, dev->sm_count, static_cast<cudaStream_t>(stream)),
+    return launch_status(launch_cache_append(p, dtype, cache_dtype, static_cast<cudaStream_t>(stream)),
                          "sdpa_cache_append");
 }
 

@@ -377,8 +377,7 @@ cudaError_t launch_cache_plan(const PlanParams &p, int sm_count, cudaStream_t st
                              dim3(kPlanThreads), 0, stream, p, row_ctas);
 }
 
-cudaError_t launch_cache_append(const AppendParams &p, int dtype, int cache_dtype, int sm_count,
-                                cudaStream_t stream) {
+cudaError_t launch_cache_append(const AppendParams &p, int dtype, int cache_dtype, cudaStream_t stream) {
     const int groups = kAppendThreads / (p.d / 8);
     // a CTA for each of its rows: a grid of 8 CTAs an SM that loops took 81 us for 60,000 tokens, this 74
     const int64_t grid = ((int64_t)p.total * p.h_kv + groups * kAppendRows - 1) / (groups * kAppendRows);

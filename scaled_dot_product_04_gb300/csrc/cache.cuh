@@ -38,8 +38,7 @@ struct AppendParams {
     int64_t k_stride, v_stride;      // elements between tokens
     int total, h_kv, d, num_pages, page_size;
 };
-cudaError_t launch_cache_append(const AppendParams &p, int dtype, int cache_dtype, int sm_count,
-                                cudaStream_t stream);
+cudaError_t launch_cache_append(const AppendParams &p, int dtype, int cache_dtype, cudaStream_t stream);
 
 // The accepted path of a verified tree, moved to the tree's front
 // (sdpa_cache_accept).

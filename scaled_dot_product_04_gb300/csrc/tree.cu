@@ -131,11 +131,7 @@ SDPA_DEV bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtx &w, uint32_
 }
 
 // ------------------------------------------------------------------ schedule
-// Tokens of a row tile, and of one chain's share of it.
-template <int kRows>
-__host__ __device__ inline int tokens_per_chain(const TreeParams &p) {
-    return p.chain_tokens;
-}
+// Tokens of a row tile; of one chain's share of it: chain_tokens.
 template <int kRows>
 __host__ __device__ inline int tokens_per_tile(const TreeParams &p) {
     return (kRows == 256 ? 2 : 1) * p.chain_tokens;
@@ -172,7 +168,7 @@ SDPA_DEV int key_tiles(int end) { return max((end + kTileN - 1) / kTileN, 1); }
 // a unit's first CTA is the one whose share holds the end of its first tile.
 template <int kRows>
 SDPA_DEV int tile_places(const TreeParams &p, const Request &r, int rt) {
-    return kRows == 256 && r.n - rt * tokens_per_tile<kRows>(p) > tokens_per_chain<kRows>(p) ? 2 : 1;
+    return kRows == 256 && r.n - rt * tokens_per_tile<kRows>(p) > p.chain_tokens ? 2 : 1;
 }
 template <int kRows>
 SDPA_DEV int unit_places(const TreeParams &p, const Request &r, int rt, int cost) {
@@ -417,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int mine = (int)lane / L::kChunks, col = (int)lane % L::kChunks;
             const bool loads = mine < pages;
             const int none = p.num_pages * p.h_kv;  // behind the last: reads as zeros
-            const int tpc = tokens_per_chain<kRows>(p);
+            const int tpc = p.chain_tokens;
             uint32_t stage = 0, phase = 0;  // the ring's next place
             bool ok = true;
             __syncthreads();
@@ -540,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             else mma_ts(o, pc, v, idesc_o, add);
                         }
                 };
-                const int tpc = tokens_per_chain<kRows>(p);
+                const int tpc = p.chain_tokens;
                 int units = 0;
                 uint32_t stage = 0, phase = 0;               // the ring's next place: tiles are used in the order they lie
                 uint32_t p_phase[2] = {0, 0}, o_phase[2] = {1, 1};  // a first wait for O's release passes
@@ -614,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         } else {
             // ======================================================== Q
-            const int tpc = tokens_per_chain<kRows>(p);
+            const int tpc = p.chain_tokens;
             int units = 0;
             __syncthreads();
             Units walk(p, *start);
@@ -733,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kKeys = kTileN / kSplit;
         const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t scol = t_lane + L::kColS + x * 128, ocol = t_lane + L::kColO + x * D;
-        const int tpc = tokens_per_chain<kRows>(p);
+        const int tpc = p.chain_tokens;
         const float *qscale = reinterpret_cast<const float *>(smem + L::kQScale);
         const float descale_v = kFp8 ? *p.descale_v : 1.f;
         const int tok_l = row / p.group;           // the row's token in the chain's tile
@@ -1153,7 +1149,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p) {
     const Cut cut = reinterpret_cast<const Cut *>(p.workspace)[blockIdx.x + 1];
     if (cut.parts == 0) return;
     const int c = blockIdx.x + 1 - cut.mine, sharers = cut.parts - 1;
-    const int rows = tokens_per_chain<kRows>(p) * p.group;  // of a chain
+    const int rows = p.chain_tokens * p.group;  // of a chain
     const int end = cut.ntok * p.group;
     const float *parts = reinterpret_cast<const float *>(p.workspace + kTreeMaxCtas * sizeof(Cut));
     const float descale = kFp8 ? *p.descale_v : 1.f;
