@@ -181,6 +181,8 @@ def attention_fp8(q, k, v, descale_q, descale_k, descale_v, *, scale=None, causa
 
 # ------------------------------------------------------------------ paged key/value cache
 # Checked and marshalled in csrc/calls.cpp: a decoding step is a few of these calls a layer.
+# What a call allocates is memory of the stream that it runs on (`stream`, or the current one),
+# kept until the current stream is through with it too.
 class CachePlan(NamedTuple):
     """What cache_plan writes.  cu_new [b + 1] and kv_lens [b] go to attention_tree, slot_map
     [max_new] to cache_append; positions [max_new]; tree_mask [max_new, mask_words] or None;

@@ -11,6 +11,7 @@
 
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -124,14 +125,6 @@ sdpa_stream_t stream_of(PyObject *o) {
     return p;
 }
 
-// The memory of `t`, which ends with the call, is not handed out again before `stream` is through with it.
-void record(const at::Tensor &t, sdpa_stream_t stream) {
-    auto s = static_cast<cudaStream_t>(stream);
-    if (s == cudaStreamLegacy) s = nullptr;
-    if (s != c10::cuda::getCurrentCUDAStream().stream())
-        c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), c10::cuda::getStreamFromExternal(s, t.get_device()));
-}
-
 void check(int status) {
     if (status != SDPA_OK) refuse(g_last_error(), status);
 }
@@ -139,8 +132,18 @@ template <class T>
 T *data(const at::Tensor *t) {
     return t ? static_cast<T *>(t->data_ptr()) : nullptr;
 }
-at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, const at::Tensor &like) {
-    return at::empty(shape, like.options().dtype(type));
+// Memory that a call allocates for the work that it puts on `stream`.  It is that stream's: memory
+// freed on the current stream may have writes to come there.  What is returned is also kept until
+// the current stream, where the caller goes on, is through with it.
+at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, const at::Tensor &like, sdpa_stream_t stream, bool returned = true) {
+    auto s = static_cast<cudaStream_t>(stream);
+    if (s == cudaStreamLegacy) s = nullptr;
+    const auto current = c10::cuda::getCurrentCUDAStream();
+    if (s == current.stream()) return at::empty(shape, like.options().dtype(type));
+    const c10::cuda::CUDAStreamGuard guard(c10::cuda::getStreamFromExternal(s, like.get_device()));
+    at::Tensor t = at::empty(shape, like.options().dtype(type));
+    if (returned) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), current);
+    return t;
 }
 
 // ------------------------------------------------------------------ the calls
@@ -163,6 +166,7 @@ PyObject *cache_plan(PyObject *const *a) {
     if (parents) dense(*parents, "parents", at::kInt, {max_new});
     const SameDevice same(ctx);
     same.all(&fresh, &held, &state, &ring, &table, parents);
+    const sdpa_stream_t stream = stream_of(a[11]);
     at::Tensor out[7];  // cu_new, kv_lens, slot_map, positions, tree_mask, held, ring_state
     const at::DimVector shapes[7] = {{b + 1}, {b}, {max_new}, {max_new}, {max_new, words}, {b}, {3}};
     static const char *names[7] = {"out.cu_new",    "out.kv_lens", "out.slot_map",  "out.positions",
@@ -179,13 +183,13 @@ PyObject *cache_plan(PyObject *const *a) {
         }
     } else {
         for (int i = 0; i < 7; ++i)
-            if (i != 4 || words > 0) out[i] = empty(shapes[i], at::kInt, ctx);
+            if (i != 4 || words > 0) out[i] = empty(shapes[i], at::kInt, ctx, stream);
     }
     using I = int32_t;
     check(g_plan(data<I>(&ctx), data<I>(&fresh), data<I>(parents), data<I>(&held), data<I>(&state), data<I>(&ring),
                  data<I>(&table), data<I>(&out[5]), data<I>(&out[6]), data<I>(&out[0]), data<I>(&out[1]), data<I>(&out[2]),
                  data<I>(&out[3]), words > 0 ? data<uint32_t>(&out[4]) : nullptr, (int)b, (int)table.size(1), page,
-                 (int)ring.size(0), max_new, words, stream_of(a[11])));
+                 (int)ring.size(0), max_new, words, stream));
     if (a[10] != Py_None) return Py_NewRef(a[10]);
     PyObject *r = PyTuple_New(7);
     for (int i = 0; r && i < 7; ++i) PyTuple_SET_ITEM(r, i, i == 4 && words == 0 ? Py_NewRef(Py_None) : THPVariable_Wrap(out[i]));
@@ -229,18 +233,19 @@ PyObject *cache_accept(PyObject *const *a) {
     if (given) dense(*given, "out", at::kInt, {b});
     const SameDevice same(kc);
     same.all(&vc, &table, &ctx, &fresh, &path, &lens, given);
-    const at::Tensor out = given ? *given : empty({b}, at::kInt, ctx);
+    const sdpa_stream_t stream = stream_of(a[8]);
+    const at::Tensor out = given ? *given : empty({b}, at::kInt, ctx, stream);
     using I = int32_t;
     check(g_accept(kc.data_ptr(), vc.data_ptr(), data<I>(&table), data<I>(&ctx), data<I>(&fresh), data<I>(&path),
                    data<I>(&lens), data<I>(&out), (int)b, (int)table.size(1), (int)path.size(1), (int)kc.size(1),
-                   (int)kc.size(3), (int)kc.size(0), (int)kc.size(2), cache, stream_of(a[8])));
+                   (int)kc.size(3), (int)kc.size(0), (int)kc.size(2), cache, stream));
     return given ? Py_NewRef(a[7]) : THPVariable_Wrap(out);
 }
 
-at::Tensor tree_workspace(const at::Tensor &q, const at::Tensor &kc, int b, int max_q, int max_kv) {
+at::Tensor tree_workspace(const at::Tensor &q, const at::Tensor &kc, int b, int max_q, int max_kv, sdpa_stream_t stream) {
     const size_t size = g_tree_ws(b, max_q, max_kv, (int)q.size(1), (int)kc.size(1), (int)kc.size(3));
     if (size == (size_t)-1) refuse("sizes that attention_tree does not take");
-    return empty({size > 0 ? (int64_t)size : 1}, at::kByte, q);
+    return empty({size > 0 ? (int64_t)size : 1}, at::kByte, q, stream, false);
 }
 
 // attention_tree_workspace(q, k_cache, num_seqs, max_seqlen_q, max_seqlen_kv)
@@ -249,7 +254,7 @@ PyObject *attention_tree_workspace(PyObject *const *a) {
     check_shape(kc, "k_cache", {-1, -1, -1, -1});
     token_stride(q, "q", -1, kc.size(3));
     return THPVariable_Wrap(tree_workspace(q, kc, integer(a[2], "num_seqs"), integer(a[3], "max_seqlen_q"),
-                                           integer(a[4], "max_seqlen_kv")));
+                                           integer(a[4], "max_seqlen_kv"), stream_of(Py_None)));
 }
 
 // attention_tree(q, k_cache, v_cache, block_table, cu_seqlens_q, kv_lens, max_seqlen_q, max_seqlen_kv,
@@ -274,6 +279,7 @@ PyObject *attention_tree(PyObject *const *a) {
     if (dv) dense(*dv, "descale_v", at::kFloat, {1});
     const SameDevice same(q);
     same.all(&kc, &vc, &table, &cu, &lens, mask, dk, dv);
+    const sdpa_stream_t stream = stream_of(a[14]);
     at::Tensor o, lse;
     const bool given = a[12] != Py_None;
     if (given) {
@@ -287,14 +293,12 @@ PyObject *attention_tree(PyObject *const *a) {
             lse = *l;
         }
     } else {
-        o = empty({total, h, d}, q.scalar_type(), q);
-        lse = empty({total, h}, at::kFloat, q);
+        o = empty({total, h, d}, q.scalar_type(), q, stream);
+        lse = empty({total, h}, at::kFloat, q, stream);
     }
     at::Tensor ws;
-    const sdpa_stream_t stream = stream_of(a[14]);
     if (a[13] == Py_None) {
-        ws = tree_workspace(q, kc, (int)b, max_q, max_kv);
-        record(ws, stream);
+        ws = tree_workspace(q, kc, (int)b, max_q, max_kv, stream);
     } else {
         ws = *tensor(a[13], "workspace");
         dense(ws, "workspace", at::kByte, {-1});

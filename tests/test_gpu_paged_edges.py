@@ -97,3 +97,61 @@ def test_plan_takes_back_no_more_pages_than_there_are(sdpa):  # noqa: F811
     assert ring[pages - 2:].tolist() == [7, 1] and ring[:3].tolist() == [4, 2, 9]
     assert (ring[3:pages - 2] == -3).all().item()
     assert table[0, :5].tolist() == [7, 1, 4, 2, 9] and not table[1:].any().item()
+
+
+# ------------------------------------------------------------------ streams
+def _behind_pending_writes(shapes, call):
+    """call(other) while the current stream, asleep, still has to write to memory that was freed since."""
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    torch.cuda._sleep(400_000_000)
+    pending = [torch.full(shape, 77, dtype=dtype, device="cuda") for shape, dtype in shapes for _ in range(4)]
+    del pending
+    got = call(other)
+    other.synchronize()
+    torch.cuda.synchronize()
+    return got
+
+
+def test_outputs_on_another_stream_are_not_what_the_current_one_still_writes(sdpa):  # noqa: F811
+    """The outputs that a call allocates are written on `stream`: memory that was freed on the current stream, whose
+    writes there are still to come, must not be handed to them."""
+    c = base._attend_case(16, [3000, 700, 64], [16, 9, 3], 8, 2, 128, 32, BF)
+    o, lse = base._call(sdpa, c)
+    mask = paged_refs.words_of(c["rows"], c["words"]).cuda()
+    table, cu, lens = base._i32(c["table"]), base._i32(c["cu"]), base._i32(c["lens"])
+    size = sdpa.attention_tree_workspace(c["q"], c["kc"], 3, 16, 3000).numel()
+    got = _behind_pending_writes([(o.shape, BF), (lse.shape, torch.float32), ((size,), torch.uint8)], lambda other: sdpa.attention_tree(
+        c["q"], c["kc"], c["vc"], table, cu, lens, 16, 3000, tree_mask=mask, scale=c["scale"], stream=other))
+    assert torch.equal(got[0], o) and torch.equal(got[1], lse)
+    # the plan's outputs and the accepted lengths
+    args = [base._i32(x) for x in ([5, 40], [20, 3], [1, 3], [0, 4, 0])]
+    ring, table = base._i32(list(range(8))), base._i32([[4, -1, -1], [5, 6, 7]])
+    want = sdpa.cache_plan(*args, ring.clone(), table.clone(), 16, 23)
+    shapes = [(x.shape, torch.int32) for x in want if x is not None]
+    got = _behind_pending_writes(shapes, lambda other: sdpa.cache_plan(*args, ring, table, 16, 23, stream=other))
+    for x, y in zip(got, want):
+        assert x is y is None or torch.equal(x, y)
+    ctx, new, path, plen = (base._i32(x) for x in ([5, 40], [20, 3], [[0, 1], [2, -1]], [2, 1]))
+    got = _behind_pending_writes([((2,), torch.int32)], lambda other: sdpa.cache_accept(
+        c["kc"], c["vc"], table, ctx, new, path, plen, stream=other))
+    assert got.tolist() == [7, 41]
+
+
+def test_outputs_of_another_stream_wait_for_the_current_one(sdpa):  # noqa: F811
+    """An output that was read on the current stream and dropped is not handed out on its own before that read."""
+    c = base._attend_case(17, [900, 64], [16, 3], 8, 2, 128, 32, BF)
+    o, _ = base._call(sdpa, c)
+    mask = paged_refs.words_of(c["rows"], c["words"]).cuda()
+    table, cu, lens = base._i32(c["table"]), base._i32(c["cu"]), base._i32(c["lens"])
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    got = sdpa.attention_tree(c["q"], c["kc"], c["vc"], table, cu, lens, 16, 900, tree_mask=mask, scale=c["scale"], stream=other)
+    torch.cuda.current_stream().wait_stream(other)
+    torch.cuda._sleep(400_000_000)
+    read = got[0].clone()
+    del got
+    with torch.cuda.stream(other):
+        taken = [torch.full(o.shape, 77, dtype=BF, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    assert torch.equal(read, o) and all((x == 77).all().item() for x in taken)
