@@ -32,3 +32,10 @@ def test_visible_pairs_closed_forms():
     assert bench.visible_pairs(s, s, 1, w) == w * (w + 1) // 2 + (s - w) * (w + 1)
     assert bench.visible_pairs(4096, s, 2, -1) == 4096 * (s - 4096) + 4096 * 4097 // 2
     assert bench.visible_pairs(300, 500, 0, -1) == 300 * 500
+
+
+def test_the_benchmark_reports_its_kernels_dram_traffic():
+    """The line's traffic, dram_gbs and dram_frac come from a capture that is named by the library's version: the
+    present version has its entry, that of the last capture as long as the kernel is the same."""
+    import scaled_dot_product_04_gb300 as sdpa
+    assert bench.TRAFFIC.get(("bwd_main", sdpa.sdpa_version()))
