@@ -93,8 +93,9 @@ TRAFFIC = {("bwd_main", "sdpa_gb300 0.4 sm_103a"): 0.81430e9 + 0.49046e9,
            ("bwd_main", "sdpa_gb300 0.23 sm_103a"): 0.84483e9 + 0.51597e9,
            # 0.24 changed the one-tile forward only
            ("bwd_main", "sdpa_gb300 0.24 sm_103a"): 0.84483e9 + 0.51597e9,
-           # 0.25 added the paged-cache calls only
-           ("bwd_main", "sdpa_gb300 0.25 sm_103a"): 0.84483e9 + 0.51597e9}
+           # 0.25 added the paged-cache calls only, 0.26 mended them
+           ("bwd_main", "sdpa_gb300 0.25 sm_103a"): 0.84483e9 + 0.51597e9,
+           ("bwd_main", "sdpa_gb300 0.26 sm_103a"): 0.84483e9 + 0.51597e9}
 
 
 def fwd_flops(w) -> float:

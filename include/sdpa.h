@@ -436,16 +436,17 @@ size_t sdpa_tree_fwd_workspace_size(int num_seqs, int max_seqlen_q,
  *   and new tokens that no row of their request sees, may hold anything, NaN
  *   included; what some row sees must be finite.  Rows of o and lse behind
  *   cu[num_seqs] are left as they were.
- *   max_seqlen_q, max_seqlen_kv : upper bounds of n and of kv_lens.  A table
- *     holds fewer than 2^31 - 128 keys a request, and a launch is refused whose
- *     key tiles of 128, by these bounds and over all row tiles, come near 2^30.
+ *   max_seqlen_q (at most total_q, as for the packed forward), max_seqlen_kv :
+ *     upper bounds of n and of kv_lens.  A table holds fewer than 2^31 - 128 keys
+ *     a request, and a launch is refused whose key tiles of 128, by these bounds
+ *     and over all row tiles, come near 2^30.
  *   P enters the second product rounded to dtype (2^-8 of itself for bf16; for
  *     fp16 2^-11, or 2^-32 of the row's largest P where that is more); its sum is
  *     taken unrounded.  E4M3 caches: see below.
  *   descale_k, descale_v : fp32 scalars in device memory for an E4M3 cache,
  *     code * descale being the value; ignored otherwise (may be NULL).  Q and
  *     P are not rounded to 8 bits but split into 8-bit terms: Q is exact to
- *     2^-18 of its row's largest value, P to 2^-7 (fp16: 2^-10) of itself, or
+ *     2^-17 of its row's largest value, P to 2^-7 (fp16: 2^-10) of itself, or
  *     2^-18 of the row's largest P where that is more (but at most 2^-3 of
  *     itself).
  * workspace : sdpa_tree_fwd_workspace_size bytes, not used by another call

@@ -243,6 +243,7 @@ def attention_tree(q, k_cache, v_cache, block_table, cu_seqlens_q, kv_lens, max_
     [b + 1], kv_lens [b] int32.  The last cu_seqlens_q[i + 1] - cu_seqlens_q[i] of a request's
     kv_lens[i] tokens are the new ones; each sees all tokens before them, and of the new ones
     those whose bits its tree_mask row names (without a mask: itself and the ones before it).
+    max_seqlen_q (at most total_q) and max_seqlen_kv bound a request's new tokens and kv_lens.
     out: (o, lse) to write to; workspace: from attention_tree_workspace."""
     return calls().attention_tree(q, k_cache, v_cache, block_table, cu_seqlens_q, kv_lens,
                                   max_seqlen_q, max_seqlen_kv, tree_mask,

@@ -40,12 +40,13 @@
 // order, so results do not change from run to run.
 //
 // Measured (GB300; b requests x n tokens, 32 heads on 8, d = 128; of the copy
-// rate 6.78 TB/s): 64 x 1, 200-8100 keys, bf16: 169 us, 97%.  16 x 32, 500-16000
-// keys: 100 us, 85%, of which the joining takes 6.  8 x 64 over 8000-32000 keys,
-// fp16: 137 us, 65% and 1.11 PFLOP/s, joining 6; 4 x 500 after 2000-12000: 76 us,
-// 0.92 PFLOP/s, joining 9: what the issuing warp leaves between products holds
-// both.  32 x 13, E4M3: 108 us, 71%: the tensor pipe is busy 56% of the time, the
-// DRAM 65%.
+// rate 6.78 TB/s): 64 x 1, 200-8100 keys, bf16: 168 us, 98%.  16 x 32, 500-16000
+// keys: 99 us, 85%, of which the joining takes 6.  8 x 64 over 8000-32000 keys,
+// fp16: 134 us, 67% and 1.14 PFLOP/s, joining 6; 4 x 500 after 2000-12000: 76 us,
+// 0.91 PFLOP/s, joining 9: the tensor pipe is busy 57% and 47% of the main kernel's
+// time, the DRAM 64% and 28%, so neither is the limit; which of S, softmax and P V
+// a chain waits for has not been taken apart.  32 x 13, E4M3: 105 us, 73%: tensor
+// pipe 56%, DRAM 66%.
 // Tried and slower: tiles asked into L2 two, four or eight ahead of the ring
 // (64 x 1: 175 -> 190, 230, 279 us); the joining by whichever CTA is last,
 // inside this kernel (its code is cold when it runs, +6 us and more); short
@@ -55,17 +56,26 @@
 // 1 issues the products, warps 2 and 3 load Q, warps 4-7 and 8-11 are the two
 // chains' softmax.
 //
+// 16-bit caches.  P enters P V in the cache's type, which is what the product
+// takes beside V: off by 2^-8 (bf16) or 2^-11 (fp16) of itself, while its sum is
+// kept in fp32.  Against 64 bits O is off by 0.0022 and 0.00029, where rounding O
+// alone leaves 0.0017 and 0.00021.
+//
 // E4M3 caches.  The tiles stay in 8 bits; Q and P enter as sums of 8-bit terms
 // instead.  Q's row is scaled by a power of two to at most 2^8 and written as
-// E4M3 hi + lo (+ lo2 for fp16, whose 11 bits need three): exact down to 2^-18
+// E4M3 hi + lo (+ lo2 for fp16, whose 11 bits need three): exact down to 2^-17
 // of the row's largest value.  P, raised by 2^8, is written as E5M2 hi, rounded,
 // and the rest as E4M3 lo: hi leaves at most 2^-3 of the power of two below P,
 // of which lo leaves 2^-4, so P is off by 2^-7 of itself; for fp16 another
 // 2^-4 of that goes to an E4M3 lo2, which leaves 2^-11, fp16's own half step
-// (O off by 0.00028 and not 0.0012; 32 x 13: 109 -> 122 us, 4 x 500: 316 -> 382).  lo's smallest step ends that at 2^-11 (2^-7 for fp16) of the row's
-// largest weight: from there on weights are off by up to 2^-18 of the largest,
-// though never more than hi's 2^-3 of themselves.  (With an E4M3 hi, those below 2^-17 would vanish, and a long
-// context has very many of them.)
+// (O off by 0.00028 and not 0.0012).  lo's smallest step ends that at 2^-11
+// (2^-7 for fp16) of the row's largest weight: from there on weights are off by
+// up to 2^-18 of the largest, though never more than hi's 2^-3 of themselves.
+// (With an E4M3 hi, those below 2^-17 would vanish, and a long context has very
+// many of them.)  The terms cost products and conversions, so the 8-bit cache
+// pays where the memory is the limit and not for many rows (us, bf16 /
+// fp16 over E4M3 beside the 16-bit cache): 64 x 1 102 / 127 beside 171, 16 x 32 89
+// beside 99; but 4 x 500 108 / 137 beside 74, 8 x 64 215 (fp16) beside 123.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
